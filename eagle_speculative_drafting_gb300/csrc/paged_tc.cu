@@ -681,6 +681,8 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
             for (int k = 0; k < 4; ++k) pm[k] = fmaxf(fmaxf(sv[c + k], sv[c + k + 4]), pm[k]);
           const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl2;
           const bool raise = mx > m_ref + kRescale;   // false while everything is masked
+          // (0 when the old maximum lies 2^126 or more below: what was summed
+          // under it vanishes from O as it does from l)
           const float corr = !raise ? 1.f : (m_ref == -INFINITY ? 0.f : tc::ex2_approx(m_ref - mx));
           if (i > 0 && __any_sync(0xffffffffu, raise && m_ref != -INFINITY)) {
 #pragma unroll 1
@@ -689,7 +691,7 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
               tc::tmem_ld32_nowait(tO + X * 128 + c * 32, o);
               tc::tmem_ld_wait32(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (corr == 0.f ? 1.f : corr));
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
               tc::tmem_st32_nowait(tO + X * 128 + c * 32, o);
             }
           }

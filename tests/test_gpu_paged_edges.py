@@ -1,0 +1,130 @@
+"""GPU: the paged-cache operators where scores jump, are infinite, or where a
+call's surroundings (streams, captures, many blocks in a row) could show.
+
+Tolerances are those of test_gpu_paged.py; where the scores are exact dot
+products (one dimension only) a score's error is that of its scaling,
+4 u32 |s|.
+"""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_paged import U32, Batch, pe  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def compare(b, out, lse, i, d=None, rows=None):
+    """Request i's rows against the 64-bit form; d: the scores' error bound
+    (None: that of a dot product of hd terms, over the finite keys)."""
+    s = torch.cat([b.slots_prefix(), b.slots(i)])
+    G, n, r0 = b.nq // b.nkv, b.n[i], b.off_h[i]
+    kk = b.k.view(-1, b.nkv, b.hd)[s].double().repeat_interleave(G, 1)
+    vv = b.v.view(-1, b.nkv, b.hd)[s].double().repeat_interleave(G, 1)
+    qq = b.q[r0:r0 + n].double()
+    seen = torch.arange(len(s), device="cuda") <= b.P + b.c[i] + torch.arange(n, device="cuda")[:, None]
+    dots = torch.where(seen, torch.einsum("rhd,khd->hrk", qq, kk) * b.scale, -math.inf)
+    top = dots.amax(-1, keepdim=True)
+    p = torch.exp(dots - top)
+    z = p.sum(-1, keepdim=True)
+    p = p / z
+    ref, A = torch.einsum("hrk,khd->rhd", p, vv), torch.einsum("hrk,khd->rhd", p, vv.abs())
+    rl = (top + torch.log(z))[..., 0].T
+    if d is None:
+        finite = torch.where(kk.isfinite(), kk.abs(), 0.0)
+        mag = torch.where(seen, torch.einsum("rhd,khd->hrk", qq.abs(), finite), 0.0).amax(-1) * b.scale
+        d = ((b.hd + 2) * U32 * mag).T
+    u, keys = torch.finfo(b.dt).eps / 2, len(s)
+    w = (2 * d + 2.0 ** -21 + 2 * keys * U32)
+    w = w[..., None] if torch.is_tensor(w) else w
+    tol = (w + (u if b.dtype == "bf16" else 0.0)) * A + u * (ref.abs() + A * w) + 1e-30
+    got = out[r0:r0 + n].double()
+    sel = slice(None) if rows is None else rows
+    ratio = ((got - ref).abs() / tol)[sel]
+    assert not ratio.isnan().any() and (ratio <= 1).all(), (i, float(ratio.nan_to_num(1e9).max()))
+    if lse is not None:
+        err = (lse[r0:r0 + n].double() - rl).abs() / (d + 2 * keys * U32 + 2.0 ** -21 + 4 * U32 * rl.abs())
+        assert (err[sel] <= 1).all(), (i, float(err[sel].max()))
+
+
+# ---------------------------------------------------------- running maximum
+def tiles_in_a_row(b):
+    """The bf16 kernel's line of key tiles, cut among its CTAs: how many tiles
+    of one unit a CTA takes, at the median over the CTAs (the kernel's costs:
+    19 a tile against one query tile, 31 against two; units 50 and 100)."""
+    G = b.nq // b.nkv
+    RT, pt, T = 128 // G, -(-b.P // 128), b.T
+    packed = -(-T // RT)
+    apart = b.B * -(-(-(-T // b.B)) // RT)
+    shared = b.P > 0 and (apart - packed) * pt > 4 * packed
+    units = []
+    if shared:
+        units += [(pt, min(2 * RT, T - r) > RT) for _ in range(b.nkv) for r in range(0, T, 2 * RT)]
+    for n, c in zip(b.n, b.c):
+        units += [((0 if shared else pt) + -(-(c + min(n, r + 2 * RT)) // 128), min(2 * RT, n - r) > RT)
+                  for _ in range(b.nkv) for r in range(0, n, 2 * RT)]
+    total = sum((100 if two else 50) + t * (31 if two else 19) for t, two in units)
+    part = total / torch.cuda.get_device_properties(0).multi_processor_count
+    best, x = {}, 0
+    for t, two in units:
+        own, w = (100, 31) if two else (50, 19)
+        count = {}
+        for i in range(t):
+            c = int((x + (own + i * w if i else 0)) / part)
+            count[c] = count.get(c, 0) + 1
+        for c, k in count.items():
+            best[c] = max(best.get(c, 0), k)
+        x += own + t * w
+    run = sorted(best.values())
+    return run[len(run) // 2], {two for _, two in units}
+
+
+JUMPS = [
+    # nq, nkv, hd, page, prefix, rows, cached; tiles a CTA takes of a unit; units of two query tiles among them
+    ((8, 8, 64, 16, 0, [1], [20000]), 6, False),
+    ((32, 8, 128, 64, 0, [4], [20000]), 6, False),
+    ((32, 8, 128, 16, 0, [64], [20000]), 6, True),
+    ((16, 8, 64, 64, 0, [200], [15000]), 6, True),
+    ((32, 8, 128, 16, 20000, [2] * 8, [5 * i for i in range(8)]), 6, False),   # packed against the prefix
+    ((32, 8, 64, 32, 20000, [1] * 64, [3 * i for i in range(64)]), 6, True),
+    ((8, 2, 128, 16, 300, [8] * 40, [2000 + 31 * i for i in range(40)]), 6, False),
+]
+
+
+@pytest.mark.parametrize("jump", [50, 100, 300])
+@pytest.mark.parametrize("case,need,two", JUMPS, ids=lambda c: str(c[:5]) if isinstance(c, tuple) else None)
+def test_maxima_that_jump_between_tiles(pe, case, need, two, jump):
+    """Scores rise by `jump` nats from a key tile to the next (16 levels, then
+    from the bottom again; the odd heads fall): what was summed under the old
+    maximum must vanish, however far below it lies."""
+    b = Batch("bf16", *case, seed=20)
+    run, kinds = tiles_in_a_row(b)
+    assert run >= need and two in kinds, (run, kinds)   # a stream meets several tiles of a unit
+    b.scale = 0.125
+    sign = 1.0 - 2.0 * (torch.arange(b.nq, device="cuda") % 2)
+    b.q.zero_()
+    b.q[:, :, 0] = 8.0 * jump * sign
+    kf, vf = b.k.view(-1, b.nkv, b.hd), b.v.view(-1, b.nkv, b.hd)
+    for s in [b.slots_prefix()] + [b.slots(i) for i in range(b.B)]:
+        tile = torch.arange(len(s), device="cuda") // 128
+        kf[s] = 0.0
+        kf[s, :, 0] = (tile % 16).to(b.dt)[:, None]
+        vf[s] += (1 + tile % 3).to(b.dt)[:, None, None]
+    pe.peagle_clear_library_status()
+    out, lse = b.attend(pe)
+    assert pe.peagle_get_library_status() == 0
+    for i in range(b.B):
+        compare(b, out, lse, i, d=4 * U32 * 15 * jump)
+
+
+@pytest.mark.parametrize("case", [(8, 2, 128, 16, 0, [3] * 64, [4000 + 9 * i for i in range(64)]),
+                                  (8, 2, 64, 64, 0, [150] * 4, [9000, 7000, 8000, 6000]),
+                                  (8, 2, 128, 32, 12000, [5] * 30, [40 * i for i in range(30)])],
+                         ids=lambda c: str(c[:5]))
+def test_sharp_scores_over_many_tiles(pe, case):
+    b = Batch("bf16", *case, qgain=30.0, seed=21)
+    assert tiles_in_a_row(b)[0] >= 4
+    out, lse = b.attend(pe)
+    for i in range(b.B):
+        compare(b, out, lse, i)
