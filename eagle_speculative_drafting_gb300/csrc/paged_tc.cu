@@ -67,7 +67,7 @@
 namespace pe {
 
 namespace pt {
-constexpr int TK = 128, THREADS = 512, SERVICE = 128, NU = 4;
+constexpr int TK = 128, THREADS = 512, SERVICE = 128, NU = 4, NREDO = 2 * NU;
 constexpr int BOX = 128 * 128;        // 128 rows x 64 bf16 columns
 constexpr float kRescale = 8.f;       // log2 headroom before the reference maximum moves
 // register shares of the scheduler's and issuer's warps, of the softmax groups
@@ -145,8 +145,12 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   volatile int* sIssued = abort_flag + 1;   // [5] ring positions the producers filled, Q copies issued
-  volatile int* sRedo = sIssued + 5;        // [2] 1 + the last unit whose stream met a non-finite hidden V
-  int* sStart = const_cast<int*>(sRedo + 2);   // [4] request the CTA begins with; its rows, cached tokens, first row
+  // [2 streams][NREDO] in slot u % NREDO 1 + unit u when its stream met a
+  // non-finite hidden V. Warps are at different units at a time: one that has
+  // still to look at unit u's mark has signed uempty for no later unit, so no
+  // unit behind u + NU is handed out and NREDO > NU slots never meet.
+  volatile int* sRedo = sIssued + 5;
+  int* sStart = const_cast<int*>(sRedo + 2 * NREDO);   // [4] request the CTA begins with; its rows, cached tokens, first row
   long long* sLL = reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(sStart + 4) + 7) & ~uintptr_t(7));  // [2 * SERVICE / 32 + 1]
 
   const int cta = blockIdx.x, nkv = a.nkv;
@@ -168,8 +172,8 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
       tc::mbar_init(&pfull[2 + i], 4);
       tc::mbar_init(&odone[i], 1);
       tc::mbar_init(&exch[i], 8);
-      sRedo[i] = 0;
     }
+    for (int i = 0; i < 2 * NREDO; ++i) sRedo[i] = 0;
     for (int i = 0; i < 5; ++i) sIssued[i] = 0;
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -630,7 +634,7 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
                 acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), z, acc);
               }
             const float2 bad = __bfloat1622float2(acc);
-            if ((bad.x != 0.f || bad.y != 0.f) && !dry) sRedo[X] = u + 1;
+            if ((bad.x != 0.f || bad.y != 0.f) && !dry) sRedo[X * NREDO + u % NREDO] = u + 1;
           }
           tc::fence_proxy_async();
         }
@@ -749,7 +753,8 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
       if (nX > 0 && !waitw(&odone[X], oX & 1)) break;
       tc::fence_after();
       if (two || X == 0 || join) {
-        const bool redo = two ? sRedo[X] == u + 1 : (sRedo[0] == u + 1 || sRedo[1] == u + 1);
+        const volatile int* mark_u = sRedo + u % NREDO;
+        const bool redo = two ? mark_u[X * NREDO] == u + 1 : (mark_u[0] == u + 1 || mark_u[NREDO] == u + 1);
         const bool direct = (d.flags & U_DIRECT) && !redo;
         if (wlive) {
           const size_t rh = (size_t)(d.row0 + j) * a.nq + d.g * p.G + hh;

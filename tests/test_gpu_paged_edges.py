@@ -128,3 +128,26 @@ def test_sharp_scores_over_many_tiles(pe, case):
     out, lse = b.attend(pe)
     for i in range(b.B):
         compare(b, out, lse, i)
+
+
+# ------------------------------------------------- hidden and infinite values
+@pytest.mark.parametrize("rows,cached", [([2, 5, 3, 9] * 500, [7, 130, 0, 300] * 500),    # units of one query tile
+                                         ([40, 70, 64, 33] * 40, [7, 130, 200, 300] * 40)])   # and of two
+def test_hidden_values_in_many_units_in_a_row(pe, rows, cached):
+    """Every request's last token holds a NaN value: the mark that one unit's
+    rows are to be computed again may not be lost to the next unit's."""
+    b = Batch("bf16", 16, 4, 64, 16, 0, rows, cached, seed=22)
+    want, _ = b.attend(pe)
+    last = torch.stack([b.slots(i)[-1] for i in range(b.B)])
+    b.v.view(-1, 4, 64)[last] = float("nan")
+    ends = torch.zeros(b.T, dtype=torch.bool, device="cuda")
+    ends[b.off[1:].long() - 1] = True
+    first = None
+    for _ in range(10):
+        out, _ = b.attend(pe)
+        assert out[ends].isnan().all() and not out[~ends].isnan().any()
+        first = out if first is None else first
+        assert torch.equal(out[~ends], first[~ends])
+    # the same rows without the NaN, each sum in another order: both within u16 A + roundings, A <= max|v|
+    A = float(b.v.nan_to_num(0).abs().max())
+    assert ((first[~ends].float() - want[~ends].float()).abs() <= 4 * 2.0 ** -8 * A).all()
