@@ -146,7 +146,7 @@ __device__ __noinline__ void paged_row_simt(const PagedAttnArgs& a, int b, const
       s = warp_sum(s) * a.scale;
       const float mn = fmaxf(m, s);
       const float c = m == -INFINITY ? 0.f : expf(m - mn);
-      const float p = expf(s - mn);
+      const float p = s == -INFINITY ? 0.f : expf(s - mn);   // (no -inf - -inf before a finite score)
       l = l * c + p;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * to_f(V[at + e]);

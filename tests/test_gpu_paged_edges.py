@@ -151,3 +151,32 @@ def test_hidden_values_in_many_units_in_a_row(pe, rows, cached):
     # the same rows without the NaN, each sum in another order: both within u16 A + roundings, A <= max|v|
     A = float(b.v.nan_to_num(0).abs().max())
     assert ((first[~ends].float() - want[~ends].float()).abs() <= 4 * 2.0 ** -8 * A).all()
+
+
+@pytest.mark.parametrize("hidden", [False, True])
+@pytest.mark.parametrize("lead", [1, 130])
+@pytest.mark.parametrize("case", [("bf16", 8, 2, 128, 16, 0, [4, 2], [200, 3000]),
+                                  ("bf16", 8, 2, 64, 32, 200, [5, 40], [3, 150]),
+                                  ("f32", 8, 2, 128, 16, 0, [4, 2], [200, 3000]),
+                                  ("f32", 10, 2, 64, 32, 200, [5, 40], [3, 150]),
+                                  ("f32", 96, 1, 64, 16, 0, [4, 2], [200, 190]),
+                                  ("f32", 96, 1, 64, 16, 140, [4, 2], [20, 190])],
+                         ids=lambda c: f"{c[0]}-q{c[1]}kv{c[2]}hd{c[3]}-x{c[5]}")
+def test_leading_keys_whose_score_is_minus_infinity(pe, case, lead, hidden):
+    """Their weight is 0 on every path, the one that computes rows again
+    (a hidden NaN value) among them."""
+    b = Batch(*case, seed=23)
+    b.q[:, :, 0] = b.q[:, :, 0].abs() + 0.5
+    kf = b.k.view(-1, b.nkv, b.hd)
+    for i in range(b.B):
+        s = torch.cat([b.slots_prefix(), b.slots(i)])[:lead]
+        kf[s] = 0.0
+        kf[s, :, 0] = -math.inf
+    if hidden:
+        for i in range(b.B):
+            b.v.view(-1, b.nkv, b.hd)[b.slots(i)[-1]] = float("nan")
+    out, lse = b.attend(pe)
+    if hidden:
+        b.n = [x - 1 for x in b.n]   # the rows before the last
+    for i in range(b.B):
+        compare(b, out, lse, i)
