@@ -1,6 +1,7 @@
 // C ABI of the P-EAGLE library: argument validation, the model handle,
 // workspace layout and the launch sequence of each entry point.
 // The arithmetic lives in gemm.cu, rows.cu and attn.cu.
+#include <float.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -854,8 +855,9 @@ peagle_status peagle_paged_attention(int32_t dtype, int32_t T, int32_t B, int32_
   if (st) return st;
   st = check_pages("paged_attention", page_size, num_pages, max_pages);
   if (st) return st;
-  // (the kernels scale by scale * log2(e) in fp32)
-  if (!(scale > 0) || !isfinite((float)(scale * 1.4426950408889634)))
+  // the kernels scale by scale * log2(e) in fp32: neither may overflow, or be
+  // rounded to 0 (a masked score of -inf times 0 is NaN)
+  if (!((float)scale >= FLT_MIN) || !isfinite((float)(scale * 1.4426950408889634)))
     FAIL(PEAGLE_ERR_INVALID_ARG, "paged_attention: scale=%g", scale);
   if (T == 0 || B == 0) return PEAGLE_OK;
   if (!q || !row_offsets || !kv_lens || !page_table || !k_pages || !v_pages || !out || (prefix_len > 0 && !prefix_pages))

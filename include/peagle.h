@@ -310,7 +310,8 @@ peagle_status peagle_paged_attention_workspace_size(int32_t dtype, int32_t T, in
  *                head h reads key head h / (num_q_heads / num_kv_heads)
  *   prefix_pages device int32 [ceil(prefix_len / page_size)], NULL when
  *                prefix_len is 0
- *   scale        of the scores, > 0 (1/sqrt(head_dim) as a rule)
+ *   scale        of the scores (1/sqrt(head_dim) as a rule): positive, and it
+ *                and its product with log2(e) normal fp32 numbers
  *   lse          device float [T, num_q_heads] out or NULL: log of the sum of
  *                exp(score) over the row's keys, for a caller that merges the
  *                result with attention over other keys

@@ -180,3 +180,15 @@ def test_leading_keys_whose_score_is_minus_infinity(pe, case, lead, hidden):
         b.n = [x - 1 for x in b.n]   # the rows before the last
     for i in range(b.B):
         compare(b, out, lse, i)
+
+
+@pytest.mark.parametrize("case", [("bf16", 8, 2, 128, 16, 40, [4, 70], [200, 10]), ("f32", 8, 2, 64, 16, 40, [4, 70], [200, 10]),
+                                  ("f32", 96, 1, 64, 16, 40, [4, 2], [200, 10])], ids=lambda c: f"{c[0]}-q{c[1]}")
+def test_smallest_scale(pe, case):
+    """The smallest scale that is taken makes every score 0 but for 2^-100:
+    a plain average of what a row sees."""
+    b = Batch(*case, seed=29)
+    b.scale = 2.0 ** -126
+    out, lse = b.attend(pe)
+    for i in range(b.B):
+        compare(b, out, lse, i, d=2.0 ** -100)
