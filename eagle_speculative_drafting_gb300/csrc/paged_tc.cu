@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
               pc.qi = qi;
               ((d.flags & U_PREFIX) ? p.qml : p.pml)[rh] = pc;
             }
-            if (direct && a.lse) a.lse[rh] = (m + __log2f(lt)) * 0.6931471805599453f;
+            if (direct && a.lse) a.lse[rh] = (m + log2f(lt)) * 0.6931471805599453f;
           }
           const int c_lo = join ? X * (HD / 2) : 0, c_n = join ? HD / 2 : HD;
           const uint32_t t0 = tO + (two ? X * 128 : 0);

@@ -192,3 +192,18 @@ def test_smallest_scale(pe, case):
     out, lse = b.attend(pe)
     for i in range(b.B):
         compare(b, out, lse, i, d=2.0 ** -100)
+
+
+def test_lse_does_not_depend_on_who_finished_the_row(pe):
+    """All scores 0: the sum is the number of keys, exactly, and lse its
+    logarithm, the same bits from a row that one CTA finishes and from one
+    that is joined from a prefix's piece and its own."""
+    keys = list(range(2, 300))
+    alone = Batch("bf16", 4, 1, 64, 16, 0, [1] * len(keys), [k - 1 for k in keys], qgain=0.0, seed=24)
+    joined = Batch("bf16", 4, 1, 64, 16, 1, [1] * len(keys), [k - 2 for k in keys], qgain=0.0, seed=24)
+    _, a = alone.attend(pe)
+    _, j = joined.attend(pe)
+    want = torch.log(torch.tensor(keys, dtype=torch.float64, device="cuda"))[:, None]
+    for x in (a, j):   # a logarithm off by a unit in the last place (2 u32), a rounded constant and product
+        assert ((x.double() - want).abs() <= 4 * U32 * want).all()
+    assert torch.equal(a, j)
