@@ -10,7 +10,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_paged import U32, Batch, pe  # noqa: F401
+from tests.test_gpu_paged import DT, U32, Batch, code, pe  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -207,3 +207,142 @@ def test_lse_does_not_depend_on_who_finished_the_row(pe):
     for x in (a, j):   # a logarithm off by a unit in the last place (2 u32), a rounded constant and product
         assert ((x.double() - want).abs() <= 4 * U32 * want).all()
     assert torch.equal(a, j)
+
+
+# ------------------------------------------------------------ surroundings
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_operators_on_a_side_stream(pe, dtype):
+    """Append and attention on another stream behind work that is still on its
+    way there: buffers are filled on that stream, and nothing runs elsewhere."""
+    b = Batch(dtype, 8, 2, 128, 16, 200, [3, 150], [40, 300], seed=25)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qkv = torch.randn(b.T, 12 * 128, generator=g, device="cuda")
+    pos = torch.arange(b.T, device="cuda", dtype=torch.int32)
+    cos, sin = (torch.empty(b.T, 64, device="cuda") for _ in range(2))
+    pe.peagle_rope_table(b.T, 128, 1e4, cos, sin)
+
+    def chain(stream):
+        q = torch.full((b.T, 8, 128), 7.0, device="cuda").to(b.dt)
+        pe.peagle_kv_append(code(pe, dtype), 0, b.T, b.B, 8, 2, 128, x, b.off, pos, cos, sin, b.T, b.ps, b.num_pages,
+                            b.max_pages, b.table, b.kv, q, b.k, b.v, stream)
+        b.q = q
+        return b.attend(pe, stream=stream)
+
+    x = qkv
+    want, wl = chain(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        x = torch.zeros_like(qkv)
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(4):
+            big = big @ big / 64   # keeps the stream busy
+        x.copy_(qkv)
+        got, gl = chain(s)
+    s.synchronize()
+    assert torch.equal(want, got) and torch.equal(wl, gl)
+
+
+def paged_setup(wl, B, prefix, own, seed):
+    """Pages of a step's caches: random K/V of the prefix and every request's
+    own tokens, in shuffled pages; also the same tokens as one list each."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    nkv, hd, ps, dt = wl.num_kv_heads, wl.head_dim, 16, DT[wl.dtype]
+    per = 12
+    total = B * per * 2 + 8
+    perm = torch.randperm(total, generator=g, device="cuda").to(torch.int32)
+    kp, vp = (torch.randn(total, ps, nkv, hd, generator=g, device="cuda").to(dt) for _ in range(2))
+    npre = -(-prefix // ps)
+    pre, table = perm[:npre].contiguous(), perm[npre:npre + B * per].view(B, per).contiguous()
+    full = perm[npre + B * per:npre + 2 * B * per].view(B, per).contiguous()
+    for t in (kp, vp):
+        f = t.view(-1, nkv, hd)
+        for b in range(B):
+            src = [pre[i // ps].long() * ps + i % ps for i in range(prefix)]
+            src += [table[b, i // ps].long() * ps + i % ps for i in range(own[b])]
+            dst = [full[b, i // ps].long() * ps + i % ps for i in range(prefix + own[b])]
+            f[torch.stack(dst)] = f[torch.stack(src)]
+    return kp, vp, pre, table, full
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_paged_loop_behind_a_prefix(pe, dtype):
+    """Three rounds of the loop behind a shared prefix against the loop whose
+    requests hold the prefix's tokens as their own. Rotary positions count the
+    prefix, kv_lens do not."""
+    import synth
+    from eagle_speculative_drafting_gb300.loop import PagedDraftLoop
+    from tests import harness
+    B, P, own = 3, 45, [40, 17, 64]
+    wl = synth.WORKLOADS["tiny_f32_decode"].scaled(dtype=dtype, batch=B)
+    model = harness.make_model(wl, synth.make_weights(wl))
+    kp, vp, pre, table, full = paged_setup(wl, B, P, own, 26)
+    lens = torch.tensor(own, dtype=torch.int32, device="cuda")
+    a = PagedDraftLoop(model, wl.K, [kp.clone()], [vp.clone()], full, lens + P)
+    p = PagedDraftLoop(model, wl.K, [kp], [vp], table, lens, pre, P)
+    for loop in (a, p):
+        loop.start([1, 2, 3], [P + x for x in own])
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for rnd in range(3):
+        aux = torch.randn(a.total_new, wl.num_aux * wl.target_hidden, generator=g, device="cuda").to(DT[dtype])
+        la, lp = (torch.empty(B, wl.K, wl.vocab, device="cuda") for _ in range(2))
+        a.draft(aux, la)
+        p.draft(aux, lp)
+        assert harness.max_abs_rel(lp.cpu().numpy(), la.cpu().numpy()) <= (1e-4 if dtype == "f32" else 2e-2)
+        p.drafts.copy_(a.drafts)   # (near ties may fall either way in bf16)
+        tgt = torch.zeros(B, wl.K + 1, dtype=torch.int32, device="cuda")
+        tgt[:, :wl.K] = a.drafts
+        for b in range(B):
+            keep = (b + rnd) % (wl.K + 1)
+            if keep < wl.K:
+                tgt[b, keep] = (a.drafts[b, keep] + 1) % wl.vocab
+        for loop in (a, p):
+            loop.verify_greedy(tgt)
+        assert torch.equal(a.kv_lens, p.kv_lens + P) and torch.equal(a.new_pos, p.new_pos)
+    assert pe.peagle_get_device_status(model.handle) == 0
+    model.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_paged_step(pe, dtype):
+    """A captured paged step replays beside eager steps of other sizes, which
+    take other workspaces, and follows the lengths that the device holds."""
+    import synth
+    from tests import harness
+    B, P, own = 3, 45, [40, 17, 64]
+    wl = synth.WORKLOADS["tiny_f32_decode"].scaled(dtype=dtype, batch=B)
+    model = harness.make_model(wl, synth.make_weights(wl))
+    kp, vp, pre, table, _ = paged_setup(wl, B, P, own, 27)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    g = torch.Generator(device="cuda").manual_seed(3)
+    aux = torch.randn(6, wl.num_aux * wl.target_hidden, generator=g, device="cuda").to(DT[dtype])
+    off, tok, pos, kv = i32([0, 1, 4, 6]), i32([3, 1, 4, 1, 5, 9]), i32([85, 62, 63, 64, 109, 110]), i32(own)
+    logits = torch.empty(B, wl.K, wl.vocab, device="cuda")
+
+    def step(logits):
+        return model.draft_step_paged(wl.K, off, aux, tok, pos, [kp], [vp], table, kv, pre, P, logits=logits)
+
+    def eager():
+        x = torch.empty_like(logits)
+        t = step(x)
+        return x, t
+
+    want, wt = eager()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        toks = step(logits)
+    for lens in (own, [30, 10, 50]):
+        kv.copy_(i32(lens))
+        pos.copy_(i32([lens[0] + P] + [lens[1] + P + j for j in range(3)] + [lens[2] + P + j for j in range(2)]))
+        want, wt = eager()
+        # a larger step between, over the same pages' scratch
+        n = 300
+        model.draft_step_paged(wl.K, i32([0, n]), aux[:1].expand(n, -1).contiguous(), tok[:1].expand(n).contiguous(),
+                               torch.arange(n, device="cuda", dtype=torch.int32), [kp.clone()], [vp.clone()],
+                               torch.arange(40, device="cuda", dtype=torch.int32)[None].contiguous(), i32([0]))
+        logits.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(logits, want) and torch.equal(toks, wt)
+    assert pe.peagle_get_device_status(model.handle) == 0
+    model.close()
