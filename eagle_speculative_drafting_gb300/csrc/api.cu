@@ -406,7 +406,7 @@ struct PagedCtx {
 // Workspace of a step with N new rows in all (at most max_new per request);
 // rows = N + B*(K-1). The one-anchor step is N = B, max_new = 1.
 // A paged step (paged) has the attention's own workspace in place of the
-// context-split partials.
+// new rows' K/V and the context-split partials.
 static void draft_layout(const peagle_config& c, int B, int K, int N, int max_new, int max_kv_len, Bump& bp,
                          DraftWs& ws, bool paged = false, int prefix = 0) {
   const size_t es = esize(c);
@@ -416,8 +416,10 @@ static void draft_layout(const peagle_config& c, int B, int K, int N, int max_ne
   ws.xin = bp.take_bytes((size_t)rows * H * es);
   ws.act = bp.take_bytes((size_t)rows * I * es);
   ws.q = bp.take_bytes((size_t)rows * nq * hd * es);
-  ws.kc = bp.take_bytes((size_t)rows * nkv * hd * es);
-  ws.vc = bp.take_bytes((size_t)rows * nkv * hd * es);
+  if (!paged) {   // a paged step's new rows go straight to the pages
+    ws.kc = bp.take_bytes((size_t)rows * nkv * hd * es);
+    ws.vc = bp.take_bytes((size_t)rows * nkv * hd * es);
+  }
   ws.ao = bp.take_bytes((size_t)rows * nq * hd * es);
   ws.h = bp.take<float>((size_t)rows * H);
   ws.resid0 = bp.take<float>((size_t)N * H);

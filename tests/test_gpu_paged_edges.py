@@ -346,3 +346,24 @@ def test_captured_paged_step(pe, dtype):
         assert torch.equal(logits, want) and torch.equal(toks, wt)
     assert pe.peagle_get_device_status(model.handle) == 0
     model.close()
+
+
+def test_paged_step_workspace_holds_what_the_step_uses(pe):
+    """fp32, per row: layer inputs, activations, q, the attention's output, the
+    residual stream, one contraction's output; and the attention's workspace."""
+    import synth
+    from tests import harness
+    wl = synth.WORKLOADS["tiny_f32_decode"]
+    model = harness.make_model(wl, synth.make_weights(wl))
+    c, B, K = model.cfg, 2, 4
+    qh, kvh = c.num_q_heads * c.head_dim, c.num_kv_heads * c.head_dim
+    for N in (2, 500, 8000):
+        rows = N + B * (K - 1)
+        part = max(N * c.hidden, rows * (qh + 2 * kvh), rows * c.hidden, rows * 2 * c.intermediate,
+                   B * K * c.draft_vocab)
+        floats = N * 3 * c.hidden + rows * (2 * c.hidden + c.intermediate + 2 * qh) + part
+        most = 4 * floats + pe.peagle_paged_attention_workspace_size(0, rows, B, c.num_q_heads, c.num_kv_heads,
+                                                                     c.head_dim, 100)
+        most += 8 * B * K * (c.draft_vocab // 8 + 64) + 20 * 256   # argmax partials; roundings to 256 bytes
+        assert pe.peagle_draft_step_paged_workspace_size(model.handle, B, K, N, 100) <= most
+    model.close()
