@@ -534,13 +534,12 @@ static peagle_status draft_step_impl(const peagle_model* m, const DecodeRows& dr
       pr.max_pages = pg->max_pages;
       pr.ps_log2 = pg->ps_log2;
       pr.num_pages = pg->num_pages;
-      if (go.splits != 1) FAIL(PEAGLE_ERR_UNSUPPORTED, "draft_step_paged: the projection has %d partial slabs", go.splits);
       KvAppendArgs ka{};
       ka.rows = pr;
       ka.nq = nq;
       ka.nkv = nkv;
       ka.hd = hd;
-      ka.in = go.out;
+      ka.in = go.out;   // (gemm_launch leaves one slab, its K slices folded)
       ka.in_ld = go.ldo;
       if (l == 0) {
         ka.in_compact = 1;
