@@ -529,6 +529,7 @@ static peagle_status draft_step_impl(const peagle_model* m, const DecodeRows& dr
       pr.T = rows;
       pr.off = dr.new_off;
       pr.extra = K - 1;
+      pr.min_new = 1;
       pr.kv_len = kv_lens;
       pr.table = pg->table;
       pr.max_pages = pg->max_pages;

@@ -164,6 +164,9 @@ __global__ void __launch_bounds__(128) paged_attn_simt(PagedAttnArgs a) {
   pdl_wait();
   const int r = blockIdx.x, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   PagedReq q;
+  if (r == 0 && blockIdx.y == 0)   // (a malformed request need not have a row)
+    for (int b = threadIdx.x; b < a.rows.B; b += blockDim.x)
+      if (!pr_request(a.rows, b, &q)) set_status(a.status, PEAGLE_DEV_BOUNDS);
   bool ok;
   const int b = pr_lookup(a.rows, r, &q, &ok);
   if (!ok || r < q.base || r >= q.base + q.n) {

@@ -17,6 +17,7 @@ struct PagedRows {
   int B, T;               // requests; rows the row arrays have room for
   const int* off;         // device [B+1], ascending
   int extra;
+  int min_new;            // new rows a request has at least (a draft step: its anchor)
   const int* kv_len;      // device [B]: own tokens cached before this step
   const int* table;       // device [B, max_pages]
   int max_pages, ps_log2, num_pages;
@@ -26,7 +27,7 @@ struct PagedReq {
 };
 __device__ __forceinline__ int pr_base(const PagedRows& p, int b) { return p.off[b] + b * p.extra; }
 // Whether request b is well formed: its rows inside [0, T], its tokens inside
-// its page table. A step with masked rows needs a new row to hang them on.
+// its page table.
 // (lo, hi, kv: off[b], off[b+1], kv_len[b])
 __device__ __forceinline__ bool pr_check(const PagedRows& p, int b, int lo, int hi, int kv, PagedReq* q) {
   q->first = lo;
@@ -34,7 +35,7 @@ __device__ __forceinline__ bool pr_check(const PagedRows& p, int b, int lo, int 
   q->base = lo + b * p.extra;
   q->n = hi - lo + p.extra;
   q->kv = kv;
-  return lo >= 0 && hi <= p.T && lo <= hi && (p.extra == 0 || hi > lo) &&
+  return lo >= 0 && hi <= p.T && lo <= hi && hi - lo >= p.min_new &&
          (long long)q->base + q->n <= p.T && kv >= 0 &&
          (long long)kv + q->n <= ((long long)p.max_pages << p.ps_log2);
 }

@@ -367,3 +367,48 @@ def test_paged_step_workspace_holds_what_the_step_uses(pe):
         most += 8 * B * K * (c.draft_vocab // 8 + 64) + 20 * 256   # argmax partials; roundings to 256 bytes
         assert pe.peagle_draft_step_paged_workspace_size(model.handle, B, K, N, 100) <= most
     model.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [1, 4])
+def test_step_flags_a_request_without_rows(pe, dtype, K):
+    """Every request of a step brings a row: one without is flagged, and the
+    others' drafts are as if it were not there."""
+    import synth
+    from tests import harness
+    wl = synth.WORKLOADS["tiny_f32_decode"].scaled(dtype=dtype, batch=3)
+    model = harness.make_model(wl, synth.make_weights(wl))
+    own = [40, 17, 64]
+    kp, vp, pre, table, _ = paged_setup(wl, 3, 45, own, 28)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    aux = torch.randn(4, wl.num_aux * wl.target_hidden, device="cuda").to(DT[dtype])
+
+    def step(off):
+        logits = torch.zeros(3, K, wl.vocab, device="cuda")
+        model.draft_step_paged(K, i32(off), aux, i32([3, 1, 4, 1]), i32([85, 86, 109, 110]), [kp.clone()], [vp.clone()],
+                               table, i32(own), pre, 45, logits=logits)
+        torch.cuda.synchronize()
+        status = pe.peagle_get_device_status(model.handle)
+        pe.peagle_clear_device_status(model.handle)
+        return logits, status
+
+    _, status = step([0, 2, 3, 4])
+    assert status == 0
+    bad, status = step([0, 2, 2, 4])
+    assert status == pe.PEAGLE_DEV_BOUNDS
+    assert bad[0].isfinite().all() and bad[2].isfinite().all()
+    model.close()
+
+
+@pytest.mark.parametrize("dtype,nq", [("bf16", 8), ("f32", 8), ("f32", 96)])
+def test_attention_flags_a_malformed_request_without_rows(pe, dtype, nq):
+    """Its lengths are wrong and it has no row: flagged on every path, and the
+    other requests' rows are right."""
+    b = Batch(dtype, nq, 1, 64, 16, 20, [3, 0, 2], [40, 5, 30], seed=30)
+    b.kv[1] = -1
+    pe.peagle_clear_library_status()
+    out, lse = b.attend(pe)
+    assert pe.peagle_get_library_status() == pe.PEAGLE_DEV_BOUNDS
+    pe.peagle_clear_library_status()
+    for i in (0, 2):
+        compare(b, out, lse, i)
