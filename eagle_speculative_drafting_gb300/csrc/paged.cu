@@ -158,6 +158,53 @@ cudaError_t launch_kv_append(int dtype, int in_dtype, const KvAppendArgs& a, cud
 // fp32 with more query heads to a key head than a query tile of the tiled
 // kernel holds: a warp per (row, head).
 constexpr int kF32Heads = 64;
+// Attention of row r, head h, by one warp: lane owns dims [lane*E, lane*E+E),
+// the keys go by one at a time with a running maximum m, sum l and weighted
+// value sum o.
+template <typename T, int E>
+__device__ __forceinline__ void paged_row_simt(const PagedAttnArgs& a, int b, const PagedReq& q, int r, int h) {
+  const int lane = threadIdx.x & 31, hd = 32 * E, g = h / (a.nq / a.nkv);
+  const T* Q = static_cast<const T*>(a.q) + ((size_t)r * a.nq + h) * hd + lane * E;
+  const T* K = static_cast<const T*>(a.k_pages);
+  const T* V = static_cast<const T*>(a.v_pages);
+  const int sh = a.rows.ps_log2, mask = (1 << sh) - 1;
+  float x[E], o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    x[e] = to_f(Q[e]);
+    o[e] = 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  bool bad = false;
+  auto keys = [&](const int* pages, int count) {
+    for (int t = 0; t < count; ++t) {
+      const int page = pages[t >> sh];
+      if (page < 0 || page >= a.rows.num_pages) {
+        bad = true;
+        continue;
+      }
+      const size_t at = ((((size_t)page << sh) + (t & mask)) * a.nkv + g) * hd + lane * E;
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s = fmaf(x[e], to_f(K[at + e]), s);
+      s = warp_sum(s) * a.scale;
+      const float mn = fmaxf(m, s);
+      const float c = m == -INFINITY ? 0.f : expf(m - mn);
+      const float p = s == -INFINITY ? 0.f : expf(s - mn);   // (no -inf - -inf before a finite score)
+      l = l * c + p;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * to_f(V[at + e]);
+      m = mn;
+    }
+  };
+  keys(a.prefix_pages, a.prefix);
+  keys(a.rows.table + (size_t)b * a.rows.max_pages, q.kv + (r - q.base) + 1);
+  if (bad && lane == 0) set_status(a.status, PEAGLE_DEV_BOUNDS);
+  T* out = static_cast<T*>(a.out) + ((size_t)r * a.nq + h) * hd + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = from_f<T>(o[e] / l);
+  if (a.lse && lane == 0) a.lse[(size_t)r * a.nq + h] = m + logf(l);
+}
 template <typename T, int E>
 __global__ void __launch_bounds__(128) paged_attn_simt(PagedAttnArgs a) {
   pdl_trigger();

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(pf::THREADS, 2) paged_attn_f32(PagedAttnArgs a
   float* sV = sK + TK * HD;        // [TK][HD] swizzled
   float* sP = sV + TK * HD;        // [TQ][LDP]
   __shared__ long long sLL[THREADS / 32 + 1];
-  __shared__ int sStart, sRedo, sSlot[2][TK];
+  __shared__ int sStart, sOdd, sSlot[2][TK];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tx = tid & 15, ty = tid >> 4;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(pf::THREADS, 2) paged_attn_f32(PagedAttnArgs a
       mm::cp_commit();
     };
     __syncthreads();   // the last piece is done with the tiles
-    if (tid == 0) sRedo = 0;
+    if (tid == 0) sOdd = 0;
     int page = 0;
     const int ahead = t0 + (tid >> 6);   // of 128 threads, the first two tiles
     if (tid < 2 * TK && ahead < t0 + nt) page = look_up(ahead, tid & (TK - 1));
@@ -229,18 +229,23 @@ __global__ void __launch_bounds__(pf::THREADS, 2) paged_attn_f32(PagedAttnArgs a
       if (more) load(a.k_pages, sK, t + 1);
       else mm::cp_commit();
       mm::cp_wait<1>();
-      __syncthreads();
-      // a token that some rows see and others do not may hold anything in V
+      // a token that some rows see and others do not may hold anything in V:
+      // its odd elements are taken out, each by the thread that copied them
       if (!pre && key0 + TK > vis0) {
         for (int e = tid; e < TK * C4; e += THREADS) {
           const int k = e / C4, c = e % C4;
           if (key0 + k >= vis0 && key0 + k < own) {
-            const float4 v = *reinterpret_cast<const float4*>(sV + at<HD>(k, c));
-            if (!(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY))
-              sRedo = 1;
+            float4* at_v = reinterpret_cast<float4*>(sV + at<HD>(k, c));
+            const float4 v = *at_v;
+            const bool x = fabsf(v.x) < INFINITY, y = fabsf(v.y) < INFINITY, z = fabsf(v.z) < INFINITY, w = fabsf(v.w) < INFINITY;
+            if (!(x && y && z && w)) {
+              *at_v = make_float4(x ? v.x : 0.f, y ? v.y : 0.f, z ? v.z : 0.f, w ? v.w : 0.f);
+              sOdd = 1;
+            }
           }
         }
       }
+      __syncthreads();
       if (wlive) {
 #pragma unroll 2
         for (int k = 0; k < TK; k += 4) {
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(pf::THREADS, 2) paged_attn_f32(PagedAttnArgs a
       else mm::cp_commit();
       if (next2) put_slot(t + 2, tid, page);
     }
-    const bool redo = sRedo != 0;
+    const bool odd = sOdd != 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(pf::THREADS, 2) paged_attn_f32(PagedAttnArgs a
       if (qi >= live) continue;
       const size_t rh = (size_t)(row0 + jr[i]) * a.nq + g * p.G + (qi - jr[i] * p.G);
       const size_t at_c = (size_t)cta * p.RP * p.G + qi;
-      const bool direct = whole && !redo;
+      const bool direct = whole && !odd;
       float* dst = direct ? static_cast<float*>(a.out) + rh * HD
                           : !begins ? p.co + at_c * HD : (prefix_unit ? p.qo : p.po) + rh * HD;
       const float f = direct ? 1.f / l[i] : 1.f;
@@ -285,9 +290,8 @@ __global__ void __launch_bounds__(pf::THREADS, 2) paged_attn_f32(PagedAttnArgs a
         *reinterpret_cast<float4*>(dst + (tx + 16 * j) * 4) =
             make_float4(o[i][j].x * f, o[i][j].y * f, o[i][j].z * f, o[i][j].w * f);
       if (tx == 0) {
-        const float mark = redo ? __uint_as_float(kPieceRedo) : direct ? __uint_as_float(kPieceDone) : m[i];
-        if (!begins) p.cml[at_c] = make_float2(mark, l[i]);
-        else (prefix_unit ? p.qml : p.pml)[rh] = Piece{mark, l[i], ctas, qi};
+        if (!begins) p.cml[at_c] = make_float2(m[i], pp_odd(l[i], odd));
+        else (prefix_unit ? p.qml : p.pml)[rh] = Piece{direct ? __uint_as_float(kPieceDone) : m[i], pp_odd(l[i], odd), ctas, qi};
         if (direct && a.lse) a.lse[rh] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
       }
     }

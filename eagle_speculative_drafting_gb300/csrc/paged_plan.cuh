@@ -20,9 +20,10 @@
 
 namespace pe {
 
-// A row's part of a unit's first piece: maximum (log2 units) and sum; the CTA
-// that has it and how many CTAs after it may have more of the unit; the row's
-// place in the unit.
+// A row's part of a unit's first piece: maximum (log2 units) and sum, whose
+// sign bit is set when the piece met infinite or NaN elements of V that only
+// some of the unit's rows see (pp_odd); the CTA that has it and how many CTAs
+// after it may have more of the unit; the row's place in the unit.
 struct __align__(16) Piece {
   float m, l;
   unsigned ctas;   // first | following << 16
@@ -49,9 +50,19 @@ struct PagedPlan {
   float* co;           // output [ncta][RP*G][hd]
   unsigned long long* cid;   // [ncta] which unit CTA c's piece continues (0: none)
 };
-// Marks in the place of a first piece's maximum: the row is finished, or has
-// to be computed again one key at a time (NaN payloads no maximum has).
-constexpr unsigned kPieceDone = 0x7fc0d0e5u, kPieceRedo = 0x7fc0ed00u;
+// Mark in the place of a first piece's maximum: the row is finished (a NaN
+// payload no maximum has).
+constexpr unsigned kPieceDone = 0x7fc0d0e5u;
+// Odd elements. A V element of a token that some rows of a unit see and others
+// do not takes part in the unit's product with weight 0 for the latter, and
+// 0 * inf or 0 * NaN is NaN. Such elements are taken out of the tile; the
+// joining kernel adds them to the rows that see their token (a weight is
+// positive: what it multiplies them by changes nothing). The sum's sign bit
+// says that there are some.
+__device__ __forceinline__ float pp_odd(float l, bool odd) {
+  return odd ? __uint_as_float(__float_as_uint(l) | 0x80000000u) : l;
+}
+__device__ __forceinline__ bool pp_is_odd(float l) { return __float_as_uint(l) >> 31; }
 
 __host__ __device__ __forceinline__ int pp_weight(const PagedPlan& p, int rows) { return rows > p.RT ? p.w2 : p.w1; }
 // cost of a unit, and where its tile i starts when the unit starts at u0
@@ -113,66 +124,19 @@ __device__ __forceinline__ int pp_cta(long long x, long long part) {
 }
 
 // -------------------------------------------------------------------------
-// Attention of row r, head h, by one warp: lane owns dims [lane*E, lane*E+E),
-// the keys go by one at a time with a running maximum m, sum l and weighted
-// value sum o.
-// -------------------------------------------------------------------------
-template <typename T, int E>
-__device__ __noinline__ void paged_row_simt(const PagedAttnArgs& a, int b, const PagedReq& q, int r, int h) {
-  const int lane = threadIdx.x & 31, hd = 32 * E, g = h / (a.nq / a.nkv);
-  const T* Q = static_cast<const T*>(a.q) + ((size_t)r * a.nq + h) * hd + lane * E;
-  const T* K = static_cast<const T*>(a.k_pages);
-  const T* V = static_cast<const T*>(a.v_pages);
-  const int sh = a.rows.ps_log2, mask = (1 << sh) - 1;
-  float x[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = to_f(Q[e]);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  auto keys = [&](const int* pages, int count) {
-    for (int t = 0; t < count; ++t) {
-      const int page = pages[t >> sh];
-      if (page < 0 || page >= a.rows.num_pages) {
-        bad = true;
-        continue;
-      }
-      const size_t at = ((((size_t)page << sh) + (t & mask)) * a.nkv + g) * hd + lane * E;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(x[e], to_f(K[at + e]), s);
-      s = warp_sum(s) * a.scale;
-      const float mn = fmaxf(m, s);
-      const float c = m == -INFINITY ? 0.f : expf(m - mn);
-      const float p = s == -INFINITY ? 0.f : expf(s - mn);   // (no -inf - -inf before a finite score)
-      l = l * c + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * to_f(V[at + e]);
-      m = mn;
-    }
-  };
-  keys(a.prefix_pages, a.prefix);
-  keys(a.rows.table + (size_t)b * a.rows.max_pages, q.kv + (r - q.base) + 1);
-  if (bad && lane == 0) set_status(a.status, PEAGLE_DEV_BOUNDS);
-  T* out = static_cast<T*>(a.out) + ((size_t)r * a.nq + h) * hd + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = from_f<T>(o[e] / l);
-  if (a.lse && lane == 0) a.lse[(size_t)r * a.nq + h] = m + logf(l);
-}
-
-// -------------------------------------------------------------------------
 // Joins the pieces of every (row, head) that the attention kernel did not
 // finish: with M the largest of their maxima, out = sum_i o_i 2^(m_i - M) /
 // sum_i l_i 2^(m_i - M). LPI lanes take one of them, 32 / LPI side by side in
 // a warp. It is bound by the latency of three loads in a row (the first
 // pieces' records, the names of the CTAs that may continue them, their
 // values), so the first pieces' values are loaded ahead of the lookups and
-// further ones several at a time.
+// further ones several at a time. The blocks an SM holds are given so that the
+// compiler spends the registers this takes, 64 to 80: left alone it packs most
+// forms into 40 to 48 and the loads go one after the other (one request of 4
+// rows 17.2 us with the attention, 15.5 so).
 // -------------------------------------------------------------------------
 template <typename T, int HD, int LPI>
-__global__ void __launch_bounds__(128) paged_combine(PagedAttnArgs a, PagedPlan p) {
+__global__ void __launch_bounds__(128, HD == 128 && LPI == 8 ? 7 : 6) paged_combine(PagedAttnArgs a, PagedPlan p) {
   pdl_trigger();
   pdl_wait();
   constexpr int IPW = 32 / LPI, E = HD / LPI;   // items of a warp, dims of a lane
@@ -183,7 +147,8 @@ __global__ void __launch_bounds__(128) paged_combine(PagedAttnArgs a, PagedPlan 
   const size_t end = (size_t)a.rows.T * a.nq, e0 = ((size_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * IPW;
   if (e0 >= end) return;
   const size_t rh = e0 + sub < end ? e0 + sub : e0;
-  const Piece none{-INFINITY, 0.f, 0u, 0}, P = p.pml[rh];
+  const Piece none{-INFINITY, 0.f, 0u, 0};
+  Piece P = p.pml[rh];
   bool open = e0 + sub < end && __float_as_uint(P.m) != kPieceDone;
   if (!__any_sync(0xffffffffu, open)) return;
   auto load = [&](const float* from, Vec (&v)[NV]) {
@@ -217,7 +182,8 @@ __global__ void __launch_bounds__(128) paged_combine(PagedAttnArgs a, PagedPlan 
       seen = rk;
     }
   }
-  bool redo = __float_as_uint(P.m) == kPieceRedo || __float_as_uint(Q.m) == kPieceRedo;
+  bool odd = pp_is_odd(P.l);   // (a prefix's tokens are seen by all)
+  P.l = fabsf(P.l);
   // a piece that saw nothing has no sum (or a NaN one, which stays)
   auto weight = [](float m, float l, float M) { return l != l ? l : (m == -INFINITY ? 0.f : exp2f(m - M)); };
   float M = fmaxf(P.m, Q.m);
@@ -249,7 +215,8 @@ __global__ void __launch_bounds__(128) paged_combine(PagedAttnArgs a, PagedPlan 
         sum = v.y;
       }
     }
-    redo |= (__ballot_sync(0xffffffffu, __float_as_uint(mi) == kPieceRedo) & group) != 0;
+    odd |= (__ballot_sync(0xffffffffu, pp_is_odd(sum)) & group) != 0;
+    sum = fabsf(sum);
     float top = mi;
 #pragma unroll
     for (int w = 1; w < LPI; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
@@ -282,7 +249,21 @@ __global__ void __launch_bounds__(128) paged_combine(PagedAttnArgs a, PagedPlan 
         for (int e = 0; e < E; ++e) o[e] += reinterpret_cast<const float*>(&v[z][e / VN])[e % VN] * w[z];
     }
   }
-  if (open && !redo) {
+  if (open && odd) {   // the unit's tokens behind its first row's, up to this row's own
+    const int last = q.kv + (r - q.base), back = min(max(P.qi, 0), p.RP * p.G - 1) / p.G;
+    for (int t = max(last - back + 1, q.kv); t <= last; ++t) {
+      const int page = a.rows.table[(size_t)b * a.rows.max_pages + (t >> a.rows.ps_log2)];
+      if (page < 0 || page >= a.rows.num_pages) continue;
+      const size_t slot = ((size_t)page << a.rows.ps_log2) + (t & ((1 << a.rows.ps_log2) - 1));
+      const T* v = static_cast<const T*>(a.v_pages) + (slot * a.nkv + g) * HD;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float x = to_f(v[(li + LPI * (e / VN)) * VN + e % VN]);
+        if (!(fabsf(x) < INFINITY)) o[e] += x;
+      }
+    }
+  }
+  if (open) {
     const float inv = 1.f / l;
     T* out = static_cast<T*>(a.out) + rh * HD;
 #pragma unroll
@@ -294,16 +275,6 @@ __global__ void __launch_bounds__(128) paged_combine(PagedAttnArgs a, PagedPlan 
       reinterpret_cast<Raw*>(out)[li + LPI * k] = *reinterpret_cast<const Raw*>(t);
     }
     if (a.lse && li == 0) a.lse[rh] = (M + log2f(l)) * 0.6931471805599453f;
-  }
-  unsigned again = __ballot_sync(0xffffffffu, open && redo && li == 0);
-  for (; again; again &= again - 1) {
-    const int src = __ffs(again) - 1;
-    PagedReq x{};
-    x.n = __shfl_sync(0xffffffffu, q.n, src);
-    x.kv = __shfl_sync(0xffffffffu, q.kv, src);
-    x.base = __shfl_sync(0xffffffffu, q.base, src);
-    paged_row_simt<T, HD / 32>(a, __shfl_sync(0xffffffffu, b, src), x, __shfl_sync(0xffffffffu, r, src),
-                               __shfl_sync(0xffffffffu, h, src));
   }
 }
 

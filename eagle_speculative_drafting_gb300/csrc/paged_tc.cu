@@ -45,7 +45,8 @@
 // Keys behind the last token of a unit may hold anything: their scores are
 // dropped and their V rows zeroed in shared memory (0 * NaN). A token that
 // some rows of a unit see and others do not may be NaN or infinite in V too;
-// such a unit is marked and its rows computed again one key at a time.
+// such elements are zeroed as well, and the joining kernel adds them to the
+// rows that see them (paged_plan.cuh).
 // Every wait is bounded; on expiry the kernel sets PEAGLE_DEV_TIMEOUT,
 // drains what it issued and returns.
 //
@@ -67,7 +68,7 @@
 namespace pe {
 
 namespace pt {
-constexpr int TK = 128, THREADS = 512, SERVICE = 128, NU = 4, NREDO = 2 * NU;
+constexpr int TK = 128, THREADS = 512, SERVICE = 128, NU = 4, NODD = 2 * NU;
 constexpr int BOX = 128 * 128;        // 128 rows x 64 bf16 columns
 constexpr float kRescale = 8.f;       // log2 headroom before the reference maximum moves
 // register shares of the scheduler's and issuer's warps, of the softmax groups
@@ -145,12 +146,12 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   volatile int* sIssued = abort_flag + 1;   // [5] ring positions the producers filled, Q copies issued
-  // [2 streams][NREDO] in slot u % NREDO 1 + unit u when its stream met a
-  // non-finite hidden V. Warps are at different units at a time: one that has
-  // still to look at unit u's mark has signed uempty for no later unit, so no
-  // unit behind u + NU is handed out and NREDO > NU slots never meet.
-  volatile int* sRedo = sIssued + 5;
-  int* sStart = const_cast<int*>(sRedo + 2 * NREDO);   // [4] request the CTA begins with; its rows, cached tokens, first row
+  // [NODD] in slot u % NODD 1 + unit u when it met odd elements of V. Warps
+  // are at different units at a time: one that has still to look at unit u's
+  // mark has signed uempty for no later unit, so no unit behind u + NU is
+  // handed out and NODD > NU slots never meet.
+  volatile int* sOdd = sIssued + 5;
+  int* sStart = const_cast<int*>(sOdd + NODD);   // [4] request the CTA begins with; its rows, cached tokens, first row
   long long* sLL = reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(sStart + 4) + 7) & ~uintptr_t(7));  // [2 * SERVICE / 32 + 1]
 
   const int cta = blockIdx.x, nkv = a.nkv;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
       tc::mbar_init(&odone[i], 1);
       tc::mbar_init(&exch[i], 8);
     }
-    for (int i = 0; i < 2 * NREDO; ++i) sRedo[i] = 0;
+    for (int i = 0; i < NODD; ++i) sOdd[i] = 0;
     for (int i = 0; i < 5; ++i) sIssued[i] = 0;
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -604,11 +605,12 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
         tc::fence_after();
         const bool pre = t < d.pt;
         const int key0 = (pre ? t : t - d.pt) * TK;
-        // keys behind the unit's last token, and tokens some of the stream's
-        // rows do not see: look at their V
+        // keys behind the unit's last token, and tokens some of the unit's rows
+        // do not see: look at their V (of two query tiles, the first stream does:
+        // its product of a key tile is issued before the second's)
         const int valid = (pre ? a.prefix : d.own) - key0;
-        const int hide = pre ? TK : d.vis0 + jX - key0;   // first key that row jX does not see
-        if (valid < TK || hide < TK) {
+        const int hide = pre ? TK : d.vis0 - key0;   // first key that the unit's first row does not see
+        if ((valid < TK || hide < TK) && !(two && X == 1)) {
           const int pos = base + vpos(tloc, d.nt), s = pos % NS;
           if (!dry) {
             ok = waitw(&kvfull[s], (pos / NS) & 1);
@@ -634,7 +636,15 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
                 acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), z, acc);
               }
             const float2 bad = __bfloat1622float2(acc);
-            if ((bad.x != 0.f || bad.y != 0.f) && !dry) sRedo[X * NREDO + u % NREDO] = u + 1;
+            if ((bad.x != 0.f || bad.y != 0.f) && !dry) {
+              sOdd[u % NODD] = u + 1;
+              uint16_t* e = reinterpret_cast<uint16_t*>(v);   // (in any order, as above)
+#pragma unroll 1
+              for (int k = 0; k < NH * 64; ++k) {
+                uint16_t* x = e + (k >> 6) * (BOX / 2) + (k & 63);
+                if ((*x & 0x7f80) == 0x7f80) *x = 0;
+              }
+            }
           }
           tc::fence_proxy_async();
         }
@@ -753,9 +763,8 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
       if (nX > 0 && !waitw(&odone[X], oX & 1)) break;
       tc::fence_after();
       if (two || X == 0 || join) {
-        const volatile int* mark_u = sRedo + u % NREDO;
-        const bool redo = two ? mark_u[X * NREDO] == u + 1 : (mark_u[0] == u + 1 || mark_u[NREDO] == u + 1);
-        const bool direct = (d.flags & U_DIRECT) && !redo;
+        const bool odd = sOdd[u % NODD] == u + 1;
+        const bool direct = (d.flags & U_DIRECT) && !odd;
         if (wlive) {
           const size_t rh = (size_t)(d.row0 + j) * a.nq + d.g * p.G + hh;
           const int qi = j * p.G + hh;
@@ -763,13 +772,12 @@ __global__ void __launch_bounds__(pt::THREADS, 1)
           float* po = !(d.flags & U_FIRST) ? p.co + at_c * HD : ((d.flags & U_PREFIX) ? p.qo : p.po) + rh * HD;
           const float inv = 1.f / lt;
           if (live && (two || X == 0)) {
-            const float mark = redo ? __uint_as_float(kPieceRedo) : direct ? __uint_as_float(kPieceDone) : m;
             if (!(d.flags & U_FIRST)) {
-              p.cml[at_c] = make_float2(mark, lt);
+              p.cml[at_c] = make_float2(m, pp_odd(lt, odd));
             } else {
               Piece pc;
-              pc.m = mark;
-              pc.l = lt;
+              pc.m = direct ? __uint_as_float(kPieceDone) : m;
+              pc.l = pp_odd(lt, odd);
               pc.ctas = d.ctas;
               pc.qi = qi;
               ((d.flags & U_PREFIX) ? p.qml : p.pml)[rh] = pc;

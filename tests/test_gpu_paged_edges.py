@@ -134,8 +134,8 @@ def test_sharp_scores_over_many_tiles(pe, case):
 @pytest.mark.parametrize("rows,cached", [([2, 5, 3, 9] * 500, [7, 130, 0, 300] * 500),    # units of one query tile
                                          ([40, 70, 64, 33] * 40, [7, 130, 200, 300] * 40)])   # and of two
 def test_hidden_values_in_many_units_in_a_row(pe, rows, cached):
-    """Every request's last token holds a NaN value: the mark that one unit's
-    rows are to be computed again may not be lost to the next unit's."""
+    """Every request's last token holds a NaN value: the mark that a unit has
+    met one may not be lost to the next unit's."""
     b = Batch("bf16", 16, 4, 64, 16, 0, rows, cached, seed=22)
     want, _ = b.attend(pe)
     last = torch.stack([b.slots(i)[-1] for i in range(b.B)])
@@ -163,8 +163,7 @@ def test_hidden_values_in_many_units_in_a_row(pe, rows, cached):
                                   ("f32", 96, 1, 64, 16, 140, [4, 2], [20, 190])],
                          ids=lambda c: f"{c[0]}-q{c[1]}kv{c[2]}hd{c[3]}-x{c[5]}")
 def test_leading_keys_whose_score_is_minus_infinity(pe, case, lead, hidden):
-    """Their weight is 0 on every path, the one that computes rows again
-    (a hidden NaN value) among them."""
+    """Their weight is 0 on every path, and where a hidden NaN value is met."""
     b = Batch(*case, seed=23)
     b.q[:, :, 0] = b.q[:, :, 0].abs() + 0.5
     kf = b.k.view(-1, b.nkv, b.hd)
@@ -412,3 +411,67 @@ def test_attention_flags_a_malformed_request_without_rows(pe, dtype, nq):
     pe.peagle_clear_library_status()
     for i in (0, 2):
         compare(b, out, lse, i)
+
+
+HIDDEN = [("bf16", 8, 2, 128, 16, 0, [5, 3], [200, 10]),            # one query tile, joined streams
+          ("bf16", 8, 2, 64, 32, 0, [9, 1, 30], [5000, 4000, 7000]),   # pieces of several CTAs
+          ("bf16", 32, 8, 128, 16, 300, [64, 150, 7], [20, 100, 600]),   # two query tiles behind a prefix
+          ("bf16", 8, 8, 64, 16, 0, [256, 130], [60, 3]),           # 256 rows to a unit
+          ("bf16", 8, 2, 128, 16, 9000, [4] * 30, [3 * i for i in range(30)]),   # packed against the prefix
+          ("bf16", 128, 1, 64, 16, 10, [3, 2], [130, 5]),
+          ("f32", 8, 2, 128, 16, 0, [5, 3], [200, 10]),
+          ("f32", 10, 2, 64, 32, 130, [70, 9, 30], [900, 40, 700])]
+
+
+@pytest.mark.parametrize("case", HIDDEN, ids=lambda c: f"{c[0]}-q{c[1]}kv{c[2]}hd{c[3]}-x{c[5]}")
+def test_hidden_elements_touch_only_their_rows_and_columns(pe, case):
+    """Infinite and NaN elements of tokens that the first rows do not see: in
+    the rows that see them their columns are what a sum with them is, and every
+    other bit of the result is as if they were finite."""
+    b = Batch(*case, seed=31)
+    vf = b.v.view(-1, b.nkv, b.hd)
+    want, wl = b.attend(pe)
+    expect = want.clone()
+    G = b.nq // b.nkv
+    for i in range(b.B):
+        n, r0 = b.n[i], b.off_h[i]
+        if n < 2:
+            continue
+        s = b.slots(i)[b.c[i]:]
+        first, last = n // 2, n - 1   # rows whose tokens get odd elements (one row when n == 2)
+        for row, col, value in ((first, 3, math.inf), (last, 3, math.inf), (first, 17, -math.inf), (last, 30, math.nan),
+                                (last, 17, math.inf if last > first else -math.inf)):
+            vf[s[row], 0, col] = value
+        heads = slice(0, G)   # of key head 0
+        expect[r0 + first:r0 + n, heads, 3] = math.inf
+        expect[r0 + first:r0 + n, heads, 17] = -math.inf
+        expect[r0 + last, heads, 30] = math.nan
+        if last > first:
+            expect[r0 + last, heads, 17] = math.nan
+    out, lse = b.attend(pe)
+    kind = torch.int16 if b.dtype == "bf16" else torch.int32
+    nan = expect.isnan()
+    assert torch.equal(out.isnan(), nan)
+    assert torch.equal(out[~nan].view(kind), expect[~nan].view(kind)) and torch.equal(lse, wl)
+
+
+def test_hidden_values_do_not_hold_up_the_batch(pe):
+    """One request's bad value behind a long prefix: the call takes about as
+    long as without it (computing the block's rows again, one key at a time,
+    took hundreds of times as long)."""
+    b = Batch("bf16", 32, 8, 128, 64, 20000, [8] * 40, [10 * i for i in range(40)], seed=32)
+
+    def time(reps=5):
+        best = 1e9
+        for _ in range(reps):
+            x, y = torch.cuda.Event(True), torch.cuda.Event(True)
+            x.record()
+            b.attend(pe)
+            y.record()
+            torch.cuda.synchronize()
+            best = min(best, x.elapsed_time(y))
+        return best
+    time()
+    plain = time()
+    b.v.view(-1, 8, 128)[b.slots(7)[-1]] = float("nan")
+    assert time() <= 5 * plain + 1.0   # ms
