@@ -11,11 +11,11 @@
 // are not there skips the arithmetic, which leaves a decode step bound by
 // the latency of its loads. Each tile's 64 cache slots are looked up once, two
 // tiles ahead, into shared memory.
-// Measured: prompts of 500 to 900 rows, 8 heads of 128, 225 us, 27 TFLOP/s (of
+// Measured: prompts of 500 to 900 rows, 8 heads of 128, 218 us, 28 TFLOP/s (of
 // about 75 by the FMA pipes; what is missing are barriers and the softmax
 // between the products); 32 requests of 4 to 8 rows x 4 heads to a key head,
-// 1000 to 4000 keys, 378 us; a step of 9 requests over 30 to 900 keys behind
-// 300 shared ones 22 us, one tile to a CTA and the joining kernel.
+// 1000 to 4000 keys, 377 us; a step of 9 requests over 30 to 900 keys behind
+// 300 shared ones 21 us, one tile to a CTA and the joining kernel.
 // Rows' maxima meet by shuffles in the 16 threads that share them; the sum is
 // kept per thread and added up once a unit.
 #include <limits.h>

@@ -281,10 +281,11 @@ __global__ void __launch_bounds__(128, HD == 128 && LPI == 8 ? 7 : 6) paged_comb
 template <typename T, int HD>
 inline void launch_combine(const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st) {
   // About one wave of warps (40 to an SM): a warp each, eight pieces in flight
-  // (one request of 4 rows, 17 pieces to a row: 16.9 us with the attention, 16
-  // lanes 17.7, eight 23.4; 5000 items 43.2, eight lanes 47.2). More: eight
-  // lanes, whose warps wait for four at once (16384 items of two or three
-  // pieces: 78.8 us, a warp each 84.5; 114000, a third of them open: 188, 203).
+  // (one request of 4 rows, 17 pieces to a row: 15.6 us with the attention, 16
+  // lanes 19.7, eight 23.9; 2000 items 26.4, 27.1, 28.6). More: eight lanes,
+  // whose warps wait for four at once (16384 items of two or three pieces: 81.1
+  // us, 16 lanes 82.2, a warp each 89.6; 114000, a third of them open: 192.6,
+  // 194.8, 217.8).
   const size_t items = (size_t)a.rows.T * a.nq;
   if (items <= (size_t)num_sms() * 40)
     launch_pdl(paged_combine<T, HD, 32>, dim3((unsigned)((items + 3) / 4)), 128, 0, st, a, p);

@@ -53,12 +53,12 @@
 // What bounds it, and what it measured (bf16, head_dim 128; measured copy
 // 6.78 TB/s, library product 1.92 PFLOP/s):
 //   64 requests x 8 rows, own contexts of 512 to 8192 tokens, 32/8 heads: the
-//     bytes of K and V, 204 us at 6.1 TB/s;
+//     bytes of K and V, 197 to 203 us at 6.1 to 6.3 TB/s;
 //   48 requests, 529 rows behind 40000 shared tokens: the softmax of a stream
 //     (two query tiles against a key tile take 2800 to 3100 cycles, their four
-//     products 2048), 290 to 315 us at 1.1 to 1.2 PFLOP/s;
-//   one request, 4 rows, 2048 tokens: latency, 17.5 us, of which the joining
-//     kernel is 6 and fetching instructions about 4.
+//     products 2048), 303 to 318 us at 1.1 to 1.2 PFLOP/s;
+//   one request, 4 rows, 2048 tokens: latency, 15.5 us, of which the joining
+//     kernel is 5.7 and fetching instructions about 4.
 // Tried and slower: two threads per row (16 softmax warps; 360 against 318 us
 // at 40000 shared tokens), P in shared memory, 64-key score tiles (a product
 // with N = 64 takes as long as one with N = 128), rows copied in the query tile.

@@ -112,7 +112,10 @@ class DraftLoop:
 class PagedDraftLoop(DraftLoop):
     """The same loop over a paged cache: request b's tokens are in the pages
     page_table[b] (room for every round's new rows and K - 1 masked rows),
-    behind the prefix_len tokens of prefix_pages that all requests share."""
+    behind the prefix_len tokens of prefix_pages that all requests share.
+    kv_lens count a request's own tokens; the positions that start() takes
+    count the prefix too (prefix_len + kv_lens when its keys were written at
+    positions 0..prefix_len-1)."""
 
     def __init__(self, model, K, k_pages, v_pages, page_table, kv_lens, prefix_pages=None, prefix_len=0, stream=None):
         super().__init__(model, K, k_pages, v_pages, None, kv_lens, 0, stream)

@@ -114,7 +114,10 @@ class Model:
         """One draft step over a paged cache: ``k_pages`` / ``v_pages`` hold one
         [num_pages, page_size, num_kv_heads, head_dim] tensor per layer and
         ``page_table`` [B, max_pages] each request's own pages; every request
-        also sees the ``prefix_len`` tokens of ``prefix_pages``."""
+        also sees the ``prefix_len`` tokens of ``prefix_pages``. The workspace
+        is the model's, rounded up to a power of two and kept for the model's
+        life (at most four times the largest call's need in all); pass fewer
+        rows a call where that is too much."""
         from . import peagle_draft_step_paged, peagle_draft_step_paged_workspace_size
         B, max_pages = page_table.shape
         total_new = new_tokens.numel()

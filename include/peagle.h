@@ -267,7 +267,8 @@ peagle_status peagle_next_context(int32_t B, int32_t K, const int32_t* draft_tok
  *                result nor written
  * Row j of request b is its own token kv_lens[b] + j. A malformed request
  * (offsets, lengths) sets PEAGLE_DEV_BOUNDS and its rows are skipped: nothing
- * is written for them. A page id outside [0, num_pages) sets
+ * is written for them (the append looks at requests that have rows only). A
+ * page id outside [0, num_pages) sets
  * PEAGLE_DEV_BOUNDS: nothing is stored to it, and an attention that meets it
  * leaves undefined values in that request's rows (in every row, when it is
  * one of the prefix). The calls without a model use the library status word.
@@ -315,7 +316,13 @@ peagle_status peagle_paged_attention_workspace_size(int32_t dtype, int32_t T, in
  *   lse          device float [T, num_q_heads] out or NULL: log of the sum of
  *                exp(score) over the row's keys, for a caller that merges the
  *                result with attention over other keys
- * Page slots that no row sees may hold anything, NaN included. The workspace
+ * Scores, maxima and sums are fp32. With a bf16 cache each weight is rounded
+ * to bf16 (2^-8 relative) before its product with the value, and the sum of
+ * the products is fp32; lse is of the weights before that rounding.
+ * Page slots that no row sees may hold anything, NaN included. An infinite or
+ * NaN element of V reaches the same element of the rows that see its token, and
+ * nothing else. The workspace
+ * (a float output for every row and head, two with a prefix that is packed)
  * belongs to one call at a time: calls that may overlap (two streams, two
  * captured graphs) take one each; its contents mean nothing between calls.
  * Every wait inside the bf16 kernel is bounded; one that runs out sets
@@ -337,8 +344,10 @@ peagle_status peagle_draft_step_paged_workspace_size(const peagle_model* model, 
  * the next step overwrites. kv_lens is unchanged (peagle_next_context
  * advances it).
  *   new_offsets, new_aux, new_tokens, new_pos, draft_tokens, logits: as
- *                peagle_draft_step_ctx (new_offsets[0] = 0); rotary positions
- *                count the prefix if it was computed with them
+ *                peagle_draft_step_ctx (new_offsets[0] = 0). kv_lens do not
+ *                count the prefix; new_pos do, when its keys were rotated by
+ *                positions 0..prefix_len-1 (a request's token t is then at
+ *                position prefix_len + t)
  *   k_pages/v_pages HOST arrays of num_layers device pointers; one page_table
  *                and one prefix_pages serve all layers
  * As for peagle_draft_step, steps of one model must not run concurrently. */
